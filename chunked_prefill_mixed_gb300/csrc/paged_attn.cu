@@ -705,6 +705,12 @@ __device__ void tile_softmax(const Params& P, const Tile& T, const TileRow& R, c
         if (T.nb > 0) {
             tmem_ld32(o_col + q, o);
             tmem_wait_ld(o);
+            // A row that sees none of the item's keys has weights of 0, and 0 times an
+            // infinite value of a key that other rows see is NaN: zeros, whatever O holds.
+            if (lo >= hi) {
+#pragma unroll
+                for (int e = 0; e < 32; ++e) o[e] = 0.f;
+            }
         } else {
 #pragma unroll
             for (int e = 0; e < 32; ++e) o[e] = 0.f;
@@ -748,7 +754,7 @@ __device__ void tile_softmax(const Params& P, const Tile& T, const TileRow& R, c
     // A row that is not finite although keys are hidden from it: 0 times an
     // infinite value of a hidden key is NaN.  Such rows again, over their own
     // keys only.
-    uint32_t again = __ballot_sync(0xffffffffu, mine && check != 0.f && lo < hi && (lo > T.kb || hi < T.ke));
+    uint32_t again = __ballot_sync(0xffffffffu, mine && check != 0.f && (lo > T.kb || hi < T.ke));
     for (; again; again &= again - 1) {
         const int src = __ffs(again) - 1;
         const int t2 = __shfl_sync(0xffffffffu, t, src), h2 = __shfl_sync(0xffffffffu, h, src);

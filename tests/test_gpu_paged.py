@@ -697,3 +697,92 @@ def test_pools_past_two_to_the_31_elements(permute):
         page = int(small["ids"][b["ptr"][s] + p // 16])
         assert np.array_equal(v64[page, :, p % 16], R.to64(v[t]))
     R.assert_attention(R.to64(out), R.attention(small, R.to64(q), k64, v64, 1 / np.sqrt(d)), "bf16")
+
+
+# ------------------------------------------------------------------ what a token does not see
+def _spoilt_values(x, s, key, value):
+    """The value row of a key of row s, all kv heads."""
+    page = int(x.b["ids"][x.b["ptr"][s] + key // 16])
+    x.vc[page, :, key % 16] = value
+
+
+def _empty_parts(x):
+    """(tokens of a tile item that see none of its keys, such items with partial rows,
+    such items without)."""
+    info, packed = x.plan.info, x.plan.dev.cpu().numpy()
+    items = packed[info.off_items:][:info.n_items * 8].reshape(-1, 8)
+    toks = packed[info.off_tokens:][:x.T * 4].reshape(-1, 4)
+    count, cut, whole = 0, 0, 0
+    for kind, _, t0, nt, _, kb, ke, part in items:
+        if kind == 0 and kb < ke:
+            t = toks[t0:t0 + nt]
+            n = int((np.maximum(t[:, 0], kb) >= np.minimum(t[:, 1], ke)).sum())
+            count, cut, whole = count + n, cut + (n > 0 and part >= 0), whole + (n > 0 and part < 0)
+    return count, cut, whole
+
+
+def _check_unspoilt(x, spoilt, what):
+    """The tokens that see none of the spoilt (row, key) pairs are as if there were none."""
+    x.call()
+    assert x.r.status() == 0
+    keep = np.array([not any(s == row and a <= j < z for row, j in spoilt)
+                     for s, p, a, z in R.intervals(x.b)])
+    assert keep.any() and not keep.all()
+    ref = R.attention(x.b, R.to64(x.q), x.k64, x.v64, 1 / np.sqrt(x.d), x.cap)
+    R.assert_attention(R.to64(x.out[:x.T])[keep], tuple(r[keep] for r in ref), x.dtype, R.to64(x.lse[:x.T])[keep], what)
+
+
+@pytest.mark.parametrize("value", [float("inf"), -float("inf"), float("nan")])
+@pytest.mark.parametrize("heads,dtype", [((4, 4, 128), "bf16"), ((8, 8, 64), "fp16"), ((8, 8, 128), "fp16")], ids=str)
+def test_later_values_of_a_cut_prompt_may_hold_anything(heads, dtype, value):
+    """Tiles of a prompt cut along the keys: early tokens see nothing of the last piece,
+    whose values the later tokens do see."""
+    rng = np.random.default_rng(41)
+    for n in (1000, 1024, 2000):
+        x = Attn(R.make_batch(rng, [n], [n]), *heads, dtype)
+        if n < 2000 and heads != (8, 8, 64):
+            assert _empty_parts(x)[1] > 0
+        for key in (200, 400, n - 1):
+            _spoilt_values(x, 0, key, value)
+        _check_unspoilt(x, [(0, 200), (0, 400), (0, n - 1)], f"{n} tokens")
+
+
+@pytest.mark.parametrize("sms", [1, 1000])
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+@pytest.mark.parametrize("heads,dtype", [((8, 2, 128), "bf16"), ((14, 2, 64), "fp16")], ids=str)
+def test_tokens_that_see_nothing_beside_tokens_that_see_anything(heads, dtype, value, sms):
+    """In one tile: tokens with no visible key (output 0, log-sum-exp -inf), tokens of
+    one document and tokens of the next, whose values hold infinities or NaN."""
+    rng = np.random.default_rng(42)
+    n, length = [120, 40], [900, 700]
+    lo = np.repeat([0, 300], n).astype(np.int32)
+    hi = np.concatenate([np.arange(z - a, z) + 1 for a, z in zip(n, length)]).astype(np.int32)
+    lo[10:30], hi[10:30] = 50, 50            # nothing
+    lo[30:60] = 820                          # the last document alone
+    hi[60:80] = 700                          # the first alone
+    lo[130:140], hi[130:140] = 5, 2          # nothing, lo past hi
+    x = Attn(R.make_batch(rng, n, length, key_lo=lo, key_hi=hi), *heads, dtype, sms=sms)
+    count, cut, whole = _empty_parts(x)
+    assert count > 0 and (whole if sms == 1 else cut) > 0
+    for s, key in ((0, 400), (0, 750), (1, 350)):
+        _spoilt_values(x, s, key, value)
+    _check_unspoilt(x, [(0, 400), (0, 750), (1, 350)], f"{sms} SMs")
+    for t in (*range(10, 30), *range(130, 140)):
+        assert not bool(x.out[t].any()) and bool((x.lse[t] == -float("inf")).all())
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("nan")])
+@pytest.mark.parametrize("heads,dtype", [((8, 2, 128), "bf16"), ((4, 4, 64), "fp16")], ids=str)
+def test_rows_that_see_nothing_of_a_shared_prefix(heads, dtype, value):
+    """Rows of a group whose first visible key is behind the shared pages, beside rows
+    that see an infinity or NaN there."""
+    rng = np.random.default_rng(43)
+    rows, pages = 24, 20
+    length = [pages * 16 + int(z) for z in rng.integers(1, 60, rows)]
+    lo = np.array([0 if r % 3 else pages * 16 for r in range(rows)], np.int32)
+    b = R.make_batch(rng, [1] * rows, length, shared=[(range(rows), pages)], key_lo=lo,
+                     group_indptr=np.array([0, rows], np.int32), group_pages=np.array([pages], np.int32))
+    x = Attn(b, *heads, dtype, sms=2)
+    assert x.plan.info.n_merge == rows and _empty_parts(x)[1] > 0
+    _spoilt_values(x, 0, 100, value)
+    _check_unspoilt(x, [(r, 100) for r in range(rows)], "group")
