@@ -241,6 +241,11 @@ class PagedRunner:
         dev = torch.from_numpy(packed).to(self.device)
         return PagedPlan(info, dev, paged_args(dev, info, self.shape, self.sm_scale))
 
+    def _stream(self, raw: int):
+        """torch's stream of a handle.  (An ExternalStream of handle 0 is a new stream
+        of torch's pool, not the default stream.)"""
+        return torch.cuda.ExternalStream(raw, self.device) if raw else torch.cuda.default_stream(self.device)
+
     def _on(self, stream, nbytes: int):
         """The raw handle of ``stream`` (None: the current one) and the workspace of calls on it."""
         current = torch._C._cuda_getCurrentRawStream(self.device.index)
@@ -250,13 +255,13 @@ class PagedRunner:
         if raw == current:
             capturing = torch.cuda.is_current_stream_capturing()
         else:
-            with torch.cuda.stream(torch.cuda.ExternalStream(raw, self.device)):
+            with torch.cuda.stream(self._stream(raw)):
                 capturing = torch.cuda.is_current_stream_capturing()
         if capturing:
             return raw, self.workspace
         w = self._others.get(raw)
         if w is None or w.numel() < nbytes:
-            with self._lock, torch.cuda.stream(torch.cuda.ExternalStream(raw, self.device)):
+            with self._lock, torch.cuda.stream(self._stream(raw)):
                 w = self._others.get(raw)
                 if w is None or w.numel() < nbytes:
                     if w is not None:
@@ -279,7 +284,7 @@ class PagedRunner:
         raw, workspace = self._on(stream, plan.workspace_bytes)
         if raw != plan.home and not workspace is self.workspace:
             # (the plan's memory was taken on another stream: not reused before this call is done)
-            plan.dev.record_stream(torch.cuda.ExternalStream(raw, self.device))
+            plan.dev.record_stream(self._stream(raw))
         args = plan.args
         if sm_scale is not None:
             args = PagedArgs.from_buffer_copy(args)

@@ -786,3 +786,34 @@ def test_rows_that_see_nothing_of_a_shared_prefix(heads, dtype, value):
     assert x.plan.info.n_merge == rows and _empty_parts(x)[1] > 0
     _spoilt_values(x, 0, 100, value)
     _check_unspoilt(x, [(r, 100) for r in range(rows)], "group")
+
+
+def test_runner_made_on_another_stream_and_called_on_the_default_one():
+    """The default stream is one of the other streams to this runner: with a workspace
+    of its own, zeroed before the first call there."""
+    import torch
+    rng = np.random.default_rng(46)
+    b = R.make_batch(rng, [1, 30], [4000, 100])
+    x = Attn(b, 8, 2, 128, "bf16", sms=400)
+    x.run()
+    want, side = x.out.clone(), torch.cuda.Stream()
+    args, more = R.plan_args(b)
+    with torch.cuda.stream(side):
+        x.r = _runner(8, 2, 128, "bf16")
+        x.r.num_sms = 400
+        x.plan = x.r.plan(*args, **more)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)
+    junk = [torch.full((1 << 18,), 255, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    del junk
+    x.out.fill_(7.0)
+    x.call()
+    torch.cuda.synchronize()
+    assert x.r.status() == 0 and torch.equal(x.out, want)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        x.call()
+    x.out.fill_(7.0)
+    g.replay()
+    torch.cuda.synchronize()
+    assert x.r.status() == 0 and torch.equal(x.out, want)

@@ -1,0 +1,89 @@
+"""CPU tests of PagedRunner's streams: which stream a call's workspace and a plan's
+memory are tied to, with stand-ins for CUDA's streams and for the library's calls."""
+import threading
+from types import SimpleNamespace
+
+import pytest
+
+torch = pytest.importorskip("torch")
+
+import chunked_prefill_mixed_gb300 as S  # noqa: E402
+from chunked_prefill_mixed_gb300 import runner as M  # noqa: E402
+
+
+class Cuda:
+    """Streams by their handles on device 0; what is made under which of them."""
+
+    def __init__(self, monkeypatch):
+        self.current, self.captured, self.zeroed = 0, set(), []
+        self.at = monkeypatch.setattr
+        self.at(torch._C, "_cuda_getCurrentRawStream", lambda device: self.current, raising=False)
+        self.at(torch.cuda, "is_current_stream_capturing", lambda: self.current in self.captured)
+        # (ExternalStream makes a stream of its own of the handle 0, as torch's does)
+        self.at(torch.cuda, "ExternalStream", lambda raw, device=None: SimpleNamespace(cuda_stream=raw or 0x999))
+        self.at(torch.cuda, "default_stream", lambda device=None: SimpleNamespace(cuda_stream=0))
+        self.at(torch.cuda, "stream", self.under)
+        self.at(torch, "zeros", self.zeros)
+
+    def under(self, stream):
+        cuda = self
+
+        class Under:
+            def __enter__(self):
+                self.was, cuda.current = cuda.current, stream.cuda_stream
+
+            def __exit__(self, *what):
+                cuda.current = self.was
+        return Under()
+
+    def zeros(self, n, dtype=None, device=None):
+        self.zeroed.append(self.current)
+        return torch.empty(n, dtype=dtype).fill_(0)
+
+
+@pytest.fixture
+def made(monkeypatch):
+    """A runner whose first stream is ``home``, the stand-ins and the library's calls."""
+    calls = []
+
+    def make(home):
+        r = object.__new__(M.PagedRunner)
+        r.device, r._home, r._retired, r._others = torch.device("cuda", 0), home, [], {}
+        r._lock, r.workspace, r.rope, r.shape = threading.Lock(), torch.empty(1 << 16, dtype=torch.uint8), 1, None
+        r._calls, r._append = SimpleNamespace(attend="attend", append="append"), None
+        monkeypatch.setattr(M, "_made", lambda call, *a: calls.append((call, a)))
+        return r, Cuda(monkeypatch), calls
+    return make
+
+
+class Memory:
+    """A plan's packed plan on the device: the streams that it was recorded for."""
+
+    def __init__(self):
+        self.recorded = []
+
+    def record_stream(self, stream):
+        self.recorded.append(stream.cuda_stream)
+
+
+def _plan(home, nbytes=1 << 12):
+    p = object.__new__(M.PagedPlan)
+    p.info, p.dev, p.args, p.home, p.tokens, p.workspace_bytes = None, Memory(), None, home, 3, nbytes
+    return p
+
+
+@pytest.mark.parametrize("call_on", [0, 0x30])
+@pytest.mark.parametrize("current", [0, 0x30, 0x70])
+def test_a_workspace_is_zeroed_on_the_stream_of_its_calls(made, call_on, current):
+    """Zeros are enqueued before the calls that need them, on the calls' own stream: the
+    default one (handle 0) too, where the runner's first stream is another."""
+    r, cuda, calls = made(0x10)
+    cuda.current = current
+    for nbytes in (1 << 12, 1 << 20):
+        r.attend(_plan(call_on, nbytes), None, None, None, None, stream=call_on)
+        assert cuda.zeroed[-1] == call_on and calls[-1][1][-1] == call_on
+    r.append(None, None, None, None, None, None, stream=call_on)
+    assert len(cuda.zeroed) == 2 and calls[-1][0] == "append" and calls[-1][1][-1] == call_on
+    cuda.captured = {call_on}
+    r.attend(_plan(call_on, 1 << 12), None, None, None, None, stream=call_on)
+    assert calls[-1][1][4] is r.workspace and r._others[call_on] is not r.workspace
