@@ -246,18 +246,20 @@ class PagedRunner:
         of torch's pool, not the default stream.)"""
         return torch.cuda.ExternalStream(raw, self.device) if raw else torch.cuda.default_stream(self.device)
 
+    def _capturing(self, raw: int, current: int) -> bool:
+        """Whether stream ``raw`` is being captured (current: the current stream's handle)."""
+        if raw == current:
+            return torch.cuda.is_current_stream_capturing()
+        with torch.cuda.stream(self._stream(raw)):
+            return torch.cuda.is_current_stream_capturing()
+
     def _on(self, stream, nbytes: int):
         """The raw handle of ``stream`` (None: the current one) and the workspace of calls on it."""
         current = torch._C._cuda_getCurrentRawStream(self.device.index)
         raw = current if stream is None else _stream_ptr(stream)
         if raw == self._home:
             return raw, self.workspace
-        if raw == current:
-            capturing = torch.cuda.is_current_stream_capturing()
-        else:
-            with torch.cuda.stream(self._stream(raw)):
-                capturing = torch.cuda.is_current_stream_capturing()
-        if capturing:
+        if self._capturing(raw, current):
             return raw, self.workspace
         w = self._others.get(raw)
         if w is None or w.numel() < nbytes:
@@ -282,8 +284,10 @@ class PagedRunner:
                stream=None, sm_scale: float | None = None) -> None:
         """Attention of a planned batch (sarathi_paged_attn)."""
         raw, workspace = self._on(stream, plan.workspace_bytes)
-        if raw != plan.home and not workspace is self.workspace:
-            # (the plan's memory was taken on another stream: not reused before this call is done)
+        if raw != plan.home and (workspace is not self.workspace or not self._capturing(
+                raw, torch._C._cuda_getCurrentRawStream(self.device.index))):
+            # (the plan's memory was taken on another stream: not reused before this call is
+            # done.  The main workspace is that of captures and of the first stream's calls.)
             plan.dev.record_stream(self._stream(raw))
         args = plan.args
         if sm_scale is not None:

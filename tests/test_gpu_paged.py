@@ -817,3 +817,28 @@ def test_runner_made_on_another_stream_and_called_on_the_default_one():
     g.replay()
     torch.cuda.synchronize()
     assert x.r.status() == 0 and torch.equal(x.out, want)
+
+
+def test_plan_made_on_another_stream_and_dropped():
+    """Made on a side stream, used on the runner's first and dropped while the call waits:
+    the side stream's next allocations leave the plan's memory alone."""
+    import torch
+    rng = np.random.default_rng(45)
+    b = R.make_batch(rng, [1, 30], [400, 100])
+    x = Attn(b, 8, 2, 128, "bf16")
+    x.run()
+    want, side = x.out.clone(), torch.cuda.Stream()
+    x.out.fill_(7.0)
+    args, more = R.plan_args(b)
+    with torch.cuda.stream(side):
+        x.plan = x.r.plan(*args, **more)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(20_000_000)
+    x.call()
+    at, n = x.plan.dev.data_ptr(), x.plan.dev.numel()
+    del x.plan
+    with torch.cuda.stream(side):
+        new = [torch.zeros(n, dtype=torch.int32, device="cuda") for _ in range(4)]
+        assert all(t.data_ptr() != at for t in new)
+    torch.cuda.synchronize()
+    assert x.r.status() == 0 and torch.equal(x.out, want)

@@ -87,3 +87,25 @@ def test_a_workspace_is_zeroed_on_the_stream_of_its_calls(made, call_on, current
     cuda.captured = {call_on}
     r.attend(_plan(call_on, 1 << 12), None, None, None, None, stream=call_on)
     assert calls[-1][1][4] is r.workspace and r._others[call_on] is not r.workspace
+
+
+@pytest.mark.parametrize("home,plan_on,call_on,captured,recorded", [
+    (0x10, 0x10, 0x10, False, False),   # made and used on the runner's first stream
+    (0x10, 0x20, 0x10, False, True),    # made on another, used on the first
+    (0x10, 0x10, 0x20, False, True),    # the other way round
+    (0x10, 0x20, 0x20, False, False),   # made and used on another
+    (0x10, 0x20, 0x30, False, True),
+    (0x10, 0x20, 0x10, True, False),    # captured: the caller keeps the plan
+    (0x10, 0x10, 0x20, True, False),
+])
+def test_a_plan_outlives_its_calls_on_other_streams(made, home, plan_on, call_on, captured, recorded):
+    """The memory of a plan is not reused before a call on another stream than the plan's
+    is done, whichever of the two is the runner's first."""
+    for given in (True, False):      # the call's stream as an argument, or the current one
+        r, cuda, calls = made(home)
+        plan = _plan(plan_on)
+        cuda.captured = {call_on} if captured else set()
+        cuda.current = 0x70 if given else call_on
+        r.attend(plan, None, None, None, None, stream=call_on if given else None)
+        assert plan.dev.recorded == ([call_on] if recorded else [])
+        assert calls[-1][0] == "attend" and calls[-1][1][-1] == call_on
