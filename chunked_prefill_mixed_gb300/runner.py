@@ -215,8 +215,12 @@ class PagedRunner:
         self.workspace = self._zeros(1 << 16)
 
     def _zeros(self, nbytes: int) -> torch.Tensor:
-        w = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
-        torch.cuda.current_stream(self.device).synchronize()
+        """A main workspace, zeroed: of the first stream's memory, whatever stream a
+        batch is planned on, as that is where its calls run."""
+        home = self._stream(self._home)
+        with torch.cuda.stream(home):
+            w = torch.zeros(nbytes, dtype=torch.uint8, device=self.device)
+        home.synchronize()
         return w
 
     def plan(self, qo_indptr, kv_page_indptr, kv_page_indices, kv_last_page_len, window: int = 0, prefix_len=None,
@@ -268,6 +272,10 @@ class PagedRunner:
                 if w is None or w.numel() < nbytes:
                     if w is not None:
                         self._retired.append(w)
+                    elif self.rope is not None:
+                        # (a runner dropped while its last calls run: the table, which is
+                        # of the first stream's memory, is not reused before they are done)
+                        self.rope.record_stream(self._stream(raw))
                     size = max(nbytes, 1 << 16, 0 if w is None else 2 * w.numel())
                     w = self._others[raw] = torch.zeros(size, dtype=torch.uint8, device=self.device)
         return raw, w

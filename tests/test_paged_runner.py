@@ -7,8 +7,21 @@ import pytest
 
 torch = pytest.importorskip("torch")
 
-import chunked_prefill_mixed_gb300 as S  # noqa: E402
 from chunked_prefill_mixed_gb300 import runner as M  # noqa: E402
+
+
+class Memory:
+    """Device memory (a packed plan, a table): the streams that it was recorded for."""
+
+    def __init__(self):
+        self.recorded = []
+
+    def record_stream(self, stream):
+        self.recorded.append(stream.cuda_stream)
+
+
+def _stream(raw):
+    return SimpleNamespace(cuda_stream=raw, synchronize=lambda: None)
 
 
 class Cuda:
@@ -20,8 +33,9 @@ class Cuda:
         self.at(torch._C, "_cuda_getCurrentRawStream", lambda device: self.current, raising=False)
         self.at(torch.cuda, "is_current_stream_capturing", lambda: self.current in self.captured)
         # (ExternalStream makes a stream of its own of the handle 0, as torch's does)
-        self.at(torch.cuda, "ExternalStream", lambda raw, device=None: SimpleNamespace(cuda_stream=raw or 0x999))
-        self.at(torch.cuda, "default_stream", lambda device=None: SimpleNamespace(cuda_stream=0))
+        self.at(torch.cuda, "ExternalStream", lambda raw, device=None: _stream(raw or 0x999))
+        self.at(torch.cuda, "default_stream", lambda device=None: _stream(0))
+        self.at(torch.cuda, "current_stream", lambda device=None: _stream(self.current))
         self.at(torch.cuda, "stream", self.under)
         self.at(torch, "zeros", self.zeros)
 
@@ -49,21 +63,11 @@ def made(monkeypatch):
     def make(home):
         r = object.__new__(M.PagedRunner)
         r.device, r._home, r._retired, r._others = torch.device("cuda", 0), home, [], {}
-        r._lock, r.workspace, r.rope, r.shape = threading.Lock(), torch.empty(1 << 16, dtype=torch.uint8), 1, None
+        r._lock, r.workspace, r.rope, r.shape = threading.Lock(), torch.empty(1 << 16, dtype=torch.uint8), Memory(), None
         r._calls, r._append = SimpleNamespace(attend="attend", append="append"), None
         monkeypatch.setattr(M, "_made", lambda call, *a: calls.append((call, a)))
         return r, Cuda(monkeypatch), calls
     return make
-
-
-class Memory:
-    """A plan's packed plan on the device: the streams that it was recorded for."""
-
-    def __init__(self):
-        self.recorded = []
-
-    def record_stream(self, stream):
-        self.recorded.append(stream.cuda_stream)
 
 
 def _plan(home, nbytes=1 << 12):
@@ -109,3 +113,21 @@ def test_a_plan_outlives_its_calls_on_other_streams(made, home, plan_on, call_on
         r.attend(plan, None, None, None, None, stream=call_on if given else None)
         assert plan.dev.recorded == ([call_on] if recorded else [])
         assert calls[-1][0] == "attend" and calls[-1][1][-1] == call_on
+
+
+@pytest.mark.parametrize("home", [0, 0x10])
+@pytest.mark.parametrize("current", [0, 0x10, 0x20])
+def test_the_runners_own_memory_outlives_its_calls(made, home, current):
+    """A runner may be dropped while its last calls run: the main workspace is of the
+    first stream's memory wherever a batch is planned, and the table is recorded once
+    for every other stream that a call runs on."""
+    r, cuda, calls = made(home)
+    cuda.current = current
+    assert not bool(r._zeros(256).any()) and cuda.zeroed == [home] and cuda.current == current
+    for call_on in (0, 0x10, 0x20, 0x10, 0):
+        r.append(None, None, None, None, None, None, stream=call_on)
+        r.attend(_plan(call_on, 1 << 20), None, None, None, None, stream=call_on)
+    assert r.rope.recorded == [s for s in (0, 0x10, 0x20) if s != home]
+    r.rope = None                    # (a runner without a table)
+    r.attend(_plan(0x40), None, None, None, None, stream=0x40)
+    assert 0x40 in r._others
