@@ -470,10 +470,16 @@ __device__ void tile_clean(const Params& P, const Tile& T, const Counts& c, uint
 // tanh), degree 3 up to 0.6 (6e-7).  Four or five multiply-adds of two lanes for
 // two scores, where the exponential and the reciprocal of tanh_abs keep the
 // special-function unit twice as long as the softmax's own exponentials do: 2048
-// tokens behind 2048 keys (32 heads, d 128) take 123 us with scores below 0.35 of the
-// cap, 134 when most warps' largest pass that, 187 when most pass 0.6 (91 uncapped).
+// tokens behind 2048 keys (32 heads, d 128, cap 30) take 121 us with queries and keys
+// of deviation 2 and 1 (scores below 0.35 of the cap), 142 with 3 and 1, 196 with 6 and
+// 1 (most warps' largest pass 0.6); 91 uncapped.
 // A warp takes it where all of a block's scores allow; scales whose seventh power
-// would leave fp32 do not.
+// would leave fp32 do not.  The scores of keys that a row does not see are left out:
+// past an item's last key they are products with whatever the ring held, and the
+// formulas differ in the last bits.  That is looked at only where the block's
+// largest score of all is above the first bound: the maximum of the seen ones costs
+// as much again (80 keys of 128 rows with a window of 500, 41.9 us; in every block with
+// a hidden key 46.5).  Left to each row instead of to the warp, 1.15 to 1.4 times the time.
 constexpr float kTanhLow = 0.35f, kTanhHigh = 0.6f;
 constexpr float kScaleLow = 2e-4f, kScaleHigh = 50.f;
 struct CapPoly {
@@ -564,6 +570,7 @@ __device__ void tile_softmax(const Params& P, const Tile& T, const TileRow& R, c
     const float mul = capped || biased ? 1.f : P.raw_scale;  // of what v holds when the weights are taken
     const bool poly = P.raw_scale >= kScaleLow && P.raw_scale <= kScaleHigh && !P.cap_fine;
     const CapPoly cp = cap_poly(P.cap2, P.raw_scale);
+    const bool idle = r >= R.rows;  // (what such a thread holds has no say)
     float m_run = -INFINITY, l_run = 0.f;
     for (int j = 0; j < T.nb; ++j) {
         const uint32_t odd = (blocks + (uint32_t)j) & 1u;
@@ -584,15 +591,28 @@ __device__ void tile_softmax(const Params& P, const Tile& T, const TileRow& R, c
 #pragma unroll
                 for (int q = 0; q < 4; ++q) am[q] = fmax3(am[q], fabsf(v[e + 2 * q]), fabsf(v[e + 2 * q + 1]));
             }
-            const float top = fmaxf(fmaxf(am[0], am[1]), fmaxf(am[2], am[3])) * P.raw_scale;
-            if (poly && __all_sync(0xffffffffu, top <= kTanhLow)) {
+            float top = fmaxf(fmaxf(am[0], am[1]), fmaxf(am[2], am[3])) * P.raw_scale;
+            bool low = __all_sync(0xffffffffu, top <= kTanhLow || idle);
+            // (else the largest that the row sees)
+            if (!low && __any_sync(0xffffffffu, key0 < lo || key0 + N > hi)) {
+                top = 0.f;
+#pragma unroll
+                for (int q = 0; q < N; q += 16) {
+                    const uint32_t seen = bit_range(lo - key0 - q, hi - key0 - q);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) top = fmaxf(top, seen & (1u << e) ? fabsf(v[q + e]) : 0.f);
+                }
+                top *= P.raw_scale;
+                low = __all_sync(0xffffffffu, top <= kTanhLow || idle);
+            }
+            if (poly && low) {
 #pragma unroll
                 for (int e = 0; e < N; e += 2) {
                     const float2 w = odd_poly(make_float2(v[e], v[e + 1]), cp.low);
                     v[e] = w.x;
                     v[e + 1] = w.y;
                 }
-            } else if (poly && __all_sync(0xffffffffu, top <= kTanhHigh)) {
+            } else if (poly && __all_sync(0xffffffffu, top <= kTanhHigh || idle)) {
 #pragma unroll
                 for (int e = 0; e < N; e += 2) {
                     const float2 w = odd_poly(make_float2(v[e], v[e + 1]), cp.high);

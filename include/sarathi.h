@@ -524,9 +524,13 @@ typedef struct sarathi_paged_args {
  * Scores, sums and the joining of split work in fp32; weights are rounded to the
  * element type before their product with V.  sm_scale, sm_scale / score_cap and
  * score_cap must stay normal fp32 numbers, also times log2(e); out must not
- * overlap q.  Neither what lies in
- * the pages past a row's kv_len nor keys and values that a token does not see
- * (infinities and NaN included) change its output.
+ * overlap q.  Neither what lies in the pages past a row's kv_len nor keys and
+ * values that a token does not see (infinities and NaN included) change its
+ * output by more than rounding.  What no token sees, and earlier calls, change no
+ * bit of it unless a value there is infinite or NaN (rows that meet one are done
+ * again, in another order); keys that only neighbouring tokens of the row see can
+ * change last bits of a capped score, whose formula goes by the largest score that
+ * 32 query rows see.
  * Asynchronous on `cuda_stream`; no allocation, no synchronisation.  Rows of out
  * and lse at or past num_tokens are left as they were.  Launches using one
  * workspace must not overlap in time (two captured graphs may share one if they

@@ -842,3 +842,42 @@ def test_plan_made_on_another_stream_and_dropped():
         assert all(t.data_ptr() != at for t in new)
     torch.cuda.synchronize()
     assert x.r.status() == 0 and torch.equal(x.out, want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("heads", [(8, 2, 128), (14, 2, 64)], ids=str)
+def test_capped_bits_do_not_depend_on_unseen_keys(heads, dtype):
+    """Keys that no token sees (before its documents, past the row's end, in other
+    requests' pages, what an earlier call left on the chip) change no bit, however large
+    they are beside the cap; keys that only later tokens see change rounding alone."""
+    import torch
+    rng = np.random.default_rng(44)
+    Hq, Hkv, d = heads
+    n, length = [200, 37, 1, 90], [333, 700, 65, 90]
+    lo = np.concatenate([[p // 64 * 64 if s == 1 else 0 for p in range(z - a, z)]
+                         for s, (a, z) in enumerate(zip(n, length))]).astype(np.int32)
+    for permute in (True, False):
+        b = R.make_batch(rng, n, length, key_lo=lo, permute=permute, spare=20)
+        x = Attn(b, Hq, Hkv, d, dtype, cap=30.0, qscale=1.0)
+        ref = x.run()
+        first, lse = x.out.clone(), x.lse.clone()
+        other = Attn(R.make_batch(rng, [300, 1], [500, 800]), Hq, Hkv, d, dtype, cap=30.0, qscale=40.0)
+        seen = {}           # (page, slot): the first token of all that sees the key
+        for t, (s, p, a, z) in enumerate(R.intervals(b)):
+            for j in range(a, z):
+                seen.setdefault((int(b["ids"][b["ptr"][s] + j // 16]), j % 16), t)
+        for trial in range(4):
+            other.call()
+            kc = torch.full_like(x.kc, float("nan")) if trial == 1 else x.kc * (60.0 if trial else 1.0)
+            keep = 120                                     # (trial 3: the keys that later tokens see are left changed)
+            for (page, slot), t in seen.items():
+                if t < keep or trial < 3:
+                    kc[page, :, slot] = x.kc[page, :, slot]
+            x.out.fill_(7.0), x.lse.fill_(7.0)
+            x.r.attend(x.plan, x.q, kc, x.vc, x.out, score_cap=x.cap, lse=x.lse)
+            torch.cuda.synchronize()
+            if trial < 3:
+                assert torch.equal(x.out, first) and torch.equal(x.lse, lse), (permute, trial)
+            else:
+                R.assert_attention(R.to64(x.out[:keep]), [y[:keep] for y in ref], dtype, R.to64(x.lse[:keep]))
+        assert x.r.status() == 0
