@@ -187,6 +187,7 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const double cap = PyFloat_AsDouble(a[8]);
         if (cap == -1.0 && PyErr_Occurred()) throw Refused();
         x.score_cap = (float)cap;
+        if (cap != 0.0 && x.score_cap == 0.f) refuse("score_cap: too small a number, 0 is no cap");
         if (a[9] != Py_None) x.slopes = static_cast<const float*>(flat("slopes", tensor("slopes", a[9]), single, heads));
         if (a[10] != Py_None) {
             const at::Tensor& lse = tensor("lse", a[10]);

@@ -373,3 +373,25 @@ def test_python_refusals():
                    dict(kv_last_page_len=[5, 5]), dict(group_pages=[1])):
         with pytest.raises(ValueError):
             S.make_paged_batch(**dict(good, **change))
+
+
+def _attend_on_cpu(**change):
+    """sarathi_paged_attn on CPU tensors, which it refuses at the end where nothing else is wrong."""
+    import torch
+    b = R.make_batch(np.random.default_rng(1), [5], [5])
+    info, packed = _plan(b, (8, 2, 64))
+    q, pool = torch.zeros(5, 8, 64, dtype=torch.bfloat16), torch.zeros(3, 2, 16, 64, dtype=torch.bfloat16)
+    a = dict(q=q, k_cache=pool, v_cache=pool, out=q.clone(), plan_dev=torch.zeros(info.packed_ints, dtype=torch.int32),
+             info=info, workspace=torch.zeros(1 << 16, dtype=torch.uint8), shape=S.Shape(8, 2, 64, 16), sm_scale=0.1)
+    a.update(change)
+    S.sarathi_paged_attn(**a)
+
+
+def test_a_cap_too_small_for_fp32_is_refused():
+    """Rounded to 0 it would stand for no cap."""
+    for cap in (1e-50, -1e-50, 1e-320):
+        with pytest.raises(ValueError, match="score_cap"):
+            _attend_on_cpu(score_cap=cap)
+    for cap in (0.0, -0.0, 1e-30, 50):
+        with pytest.raises(ValueError, match="CUDA device"):
+            _attend_on_cpu(score_cap=cap)
