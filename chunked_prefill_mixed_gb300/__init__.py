@@ -472,6 +472,8 @@ def make_paged_batch(qo_indptr, kv_page_indptr, kv_page_indices, kv_last_page_le
         raise ValueError("qo_indptr and kv_page_indptr need one entry more than there are rows, kv_last_page_len one a row")
     if kvp[-1] > ids.size:
         raise ValueError("kv_page_indices is shorter than kv_page_indptr says")
+    if not -2 ** 31 <= window < 2 ** 31:
+        raise ValueError("window outside int32")
     b = PagedBatch(n_rows=n, window=window)
     keep = [qo, kvp, ids, last]
     b.qo_indptr, b.kv_page_indptr, b.kv_page_indices, b.kv_last_page_len = (x.ctypes.data for x in keep)
@@ -495,6 +497,8 @@ def make_paged_batch(qo_indptr, kv_page_indptr, kv_page_indices, kv_last_page_le
 
 def sarathi_shared_prefix(batch: PagedBatch, min_pages: int = 1):
     """(group_indptr, group_pages) of the runs of rows that share leading pages."""
+    if not -2 ** 31 <= min_pages < 2 ** 31:
+        raise ValueError("min_pages outside int32")
     gi = np.zeros(batch.n_rows + 1, dtype=np.int32)
     gp = np.zeros(max(1, batch.n_rows), dtype=np.int32)
     n = ctypes.c_int32(0)

@@ -395,3 +395,18 @@ def test_a_cap_too_small_for_fp32_is_refused():
     for cap in (0.0, -0.0, 1e-30, 50):
         with pytest.raises(ValueError, match="CUDA device"):
             _attend_on_cpu(score_cap=cap)
+
+
+def test_a_window_or_page_count_outside_int32_is_refused():
+    """They would wrap: a window of 2^32 + 3 keys to one of 3."""
+    good = dict(qo_indptr=[0, 5], kv_page_indptr=[0, 1], kv_page_indices=[0], kv_last_page_len=[5])
+    for window in (2 ** 31, 2 ** 32 + 3, -2 ** 32 + 3):
+        with pytest.raises(ValueError, match="window"):
+            S.make_paged_batch(**good, window=window)
+    batch, keep = S.make_paged_batch(**good, window=2 ** 31 - 1)
+    assert batch.window == 2 ** 31 - 1
+    info, packed = S.sarathi_paged_plan(batch, S.Shape(8, 2, 128, 16), 152)
+    assert info.pairs == 15
+    for pages in (2 ** 31, 2 ** 32 + 1):
+        with pytest.raises(ValueError, match="min_pages"):
+            S.sarathi_shared_prefix(batch, pages)
