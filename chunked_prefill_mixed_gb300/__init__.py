@@ -513,6 +513,8 @@ def sarathi_paged_plan(batch: PagedBatch, shape: Shape, num_sms: int, host_buf: 
     info = PagedInfo()
     if host_buf is None:
         host_buf = np.zeros(0, dtype=np.int32)
+    elif host_buf.dtype != np.int32 or host_buf.ndim != 1 or not host_buf.flags.c_contiguous or not host_buf.flags.writeable:
+        raise ValueError("host_buf: a contiguous one-dimensional int32 array that can be written")
     for attempt in range(2):
         st = load().sarathi_paged_plan(ctypes.byref(batch), ctypes.byref(shape), num_sms, host_buf.ctypes.data,
                                        host_buf.nbytes, ctypes.byref(info))

@@ -410,3 +410,19 @@ def test_a_window_or_page_count_outside_int32_is_refused():
     for pages in (2 ** 31, 2 ** 32 + 1):
         with pytest.raises(ValueError, match="min_pages"):
             S.sarathi_shared_prefix(batch, pages)
+
+
+def test_a_buffer_that_cannot_hold_a_plan_as_int32_is_refused():
+    """Its words would be read as other numbers, or from between them."""
+    args, _ = R.plan_args(_good())
+    batch, keep = S.make_paged_batch(*args)
+    shape, fixed = S.Shape(8, 2, 128, 16), np.zeros(1 << 14, np.int32)
+    fixed.flags.writeable = False
+    for buf in (np.zeros(1 << 14, np.int64), np.zeros(1 << 14, np.int32)[::2], np.zeros((2, 1 << 13), np.int32), fixed,
+                np.zeros(1 << 14, np.uint8)):
+        with pytest.raises(ValueError, match="host_buf"):
+            S.sarathi_paged_plan(batch, shape, 152, buf)
+        assert not buf.any()
+    want = S.sarathi_paged_plan(batch, shape, 152)[1]
+    for n in (8, 1 << 14):      # (too small: a larger one is taken)
+        assert np.array_equal(S.sarathi_paged_plan(batch, shape, 152, np.zeros(n, np.int32))[1], want)
