@@ -116,8 +116,8 @@ PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor &kc = tensor("k_cache", a[5]), &vc = tensor("v_cache", a[6]);
         const at::Tensor &slots = tensor("slots", a[7]), &positions = tensor("positions", a[8]);
         const int64_t d = x.shape.head_dim;
-        if (ws.nbytes() < 256 || ws.get_device() != dev)
-            refuse("workspace: at least 256 bytes on the device of the others");
+        if (ws.nbytes() < 256 || ws.get_device() != dev || !ws.is_contiguous())
+            refuse("workspace: contiguous, at least 256 bytes on the device of the others");
         const Like l = element_type(k, dev, &x.dtype), whole{at::kInt, dev};
         const int64_t T = token_rows("k", k, l, x.shape.num_heads_kv, d, &x.k_stride);
         if (token_rows("v", v, l, x.shape.num_heads_kv, d, &x.v_stride) != T)
@@ -176,7 +176,8 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n) {
         const at::Tensor &ws = tensor("workspace", a[3]), &q = tensor("q", a[4]);
         const at::Tensor &kc = tensor("k_cache", a[5]), &vc = tensor("v_cache", a[6]), &out = tensor("out", a[7]);
         const int64_t heads = x.shape.num_heads_q, d = x.shape.head_dim;
-        if (ws.get_device() != dev) refuse("workspace: on the device of the others");
+        if (ws.get_device() != dev || !ws.is_contiguous())
+            refuse("workspace: contiguous, on the device of the others");
         const Like l = element_type(q, dev, &x.dtype), single{at::kFloat, dev};
         int64_t stride;
         if (token_rows("q", q, l, heads, d, &x.q_stride) < tokens)

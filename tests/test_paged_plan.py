@@ -426,3 +426,18 @@ def test_a_buffer_that_cannot_hold_a_plan_as_int32_is_refused():
     want = S.sarathi_paged_plan(batch, shape, 152)[1]
     for n in (8, 1 << 14):      # (too small: a larger one is taken)
         assert np.array_equal(S.sarathi_paged_plan(batch, shape, 152, np.zeros(n, np.int32))[1], want)
+
+
+def test_a_workspace_of_fewer_bytes_than_elements_is_refused():
+    """An expanded tensor has many elements in a few bytes of memory: the kernels would
+    write past them."""
+    import torch
+    one = torch.zeros(1, dtype=torch.uint8)
+    for ws in (one.expand(1 << 16), torch.zeros(1 << 17, dtype=torch.uint8)[::2], one.expand(256, 256)):
+        with pytest.raises(ValueError, match="workspace"):
+            _attend_on_cpu(workspace=ws)
+        k, pool = torch.zeros(5, 2, 64, dtype=torch.bfloat16), torch.zeros(3, 2, 16, 64, dtype=torch.bfloat16)
+        slots = torch.zeros(5, dtype=torch.int32)
+        with pytest.raises(ValueError, match="workspace"):
+            S.sarathi_rope_append(k, k, pool, pool, slots, slots, torch.zeros(2 * 10 * 64, dtype=torch.float64), 10,
+                                  S.Shape(8, 2, 64, 16), ws)
