@@ -252,8 +252,8 @@ class PagedRunner:
 
     def _capturing(self, raw: int, current: int) -> bool:
         """Whether stream ``raw`` is being captured (current: the current stream's handle)."""
-        if raw == current:
-            return torch.cuda.is_current_stream_capturing()
+        if raw == current and torch._C._cuda_getDevice() == self.device.index:
+            return torch.cuda.is_current_stream_capturing()  # (asks the current device)
         with torch.cuda.stream(self._stream(raw)):
             return torch.cuda.is_current_stream_capturing()
 

@@ -25,13 +25,14 @@ def _stream(raw):
 
 
 class Cuda:
-    """Streams by their handles on device 0; what is made under which of them."""
+    """Streams by their handles, all of device 0; what is made under which of them."""
 
     def __init__(self, monkeypatch):
-        self.current, self.captured, self.zeroed = 0, set(), []
+        self.current, self.device, self.captured, self.zeroed = 0, 0, set(), []
         self.at = monkeypatch.setattr
         self.at(torch._C, "_cuda_getCurrentRawStream", lambda device: self.current, raising=False)
-        self.at(torch.cuda, "is_current_stream_capturing", lambda: self.current in self.captured)
+        self.at(torch.cuda, "is_current_stream_capturing", lambda: self.device == 0 and self.current in self.captured)
+        self.at(torch._C, "_cuda_getDevice", lambda: self.device, raising=False)
         # (ExternalStream makes a stream of its own of the handle 0, as torch's does)
         self.at(torch.cuda, "ExternalStream", lambda raw, device=None: _stream(raw or 0x999))
         self.at(torch.cuda, "default_stream", lambda device=None: _stream(0))
@@ -44,10 +45,11 @@ class Cuda:
 
         class Under:
             def __enter__(self):
-                self.was, cuda.current = cuda.current, stream.cuda_stream
+                self.was = cuda.device, cuda.current
+                cuda.device, cuda.current = 0, stream.cuda_stream
 
             def __exit__(self, *what):
-                cuda.current = self.was
+                cuda.device, cuda.current = self.was
         return Under()
 
     def zeros(self, n, dtype=None, device=None):
@@ -131,3 +133,13 @@ def test_the_runners_own_memory_outlives_its_calls(made, home, current):
     r.rope = None                    # (a runner without a table)
     r.attend(_plan(0x40), None, None, None, None, stream=0x40)
     assert 0x40 in r._others
+
+
+@pytest.mark.parametrize("given", [True, False])
+@pytest.mark.parametrize("call_on", [0, 0x20])
+def test_a_capture_is_seen_from_another_device(made, call_on, given):
+    """Whether a call is captured is asked of the runner's device, not of the current one."""
+    r, cuda, calls = made(0x10)
+    cuda.device, cuda.current, cuda.captured = 1, call_on, {call_on}
+    r.attend(_plan(0x10), None, None, None, None, stream=call_on if given else None)
+    assert calls[-1][1][4] is r.workspace and not r._others and cuda.device == 1
