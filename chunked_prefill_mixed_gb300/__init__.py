@@ -142,7 +142,7 @@ def load(build_if_missing: bool = True):
     if _lib is not None:
         return _lib
     if build_if_missing and _build.stale():
-        _build.build()
+        _build.build(calls=False)
     if not os.path.exists(_build.LIB):
         raise ImportError(f"libsarathi.so not built at {_build.LIB}")
     lib = ctypes.CDLL(_build.LIB)
@@ -531,7 +531,7 @@ _calls = None   # the extension module with the two calls
 
 def paged_calls():
     """The extension module that checks the tensors of a paged call and makes it
-    (built where it is missing); imports torch."""
+    (built where it is missing; ImportError where it cannot be); imports torch."""
     global _torch, _calls
     if _calls is not None:
         return _calls
@@ -540,6 +540,8 @@ def paged_calls():
     from . import build as b
     if b.stale(b.CALLS, b.CALLS_SOURCES + b.HEADERS[:1]):
         b.build()
+    if not os.path.exists(b.CALLS):
+        raise ImportError(f"{os.path.basename(b.CALLS)} not built: {b.calls_need() or 'compiler'} missing")
     spec = importlib.util.spec_from_file_location("_paged_calls", b.CALLS)
     calls = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(calls)

@@ -4,6 +4,7 @@ from __future__ import annotations
 
 import importlib.util
 import os
+import shutil
 import subprocess
 import sys
 import sysconfig
@@ -37,31 +38,52 @@ def _start(cmd: list, target: str):
     return subprocess.Popen(cmd + ["-o", tmp]), tmp, target
 
 
+def _torch_dir() -> str:
+    spec = importlib.util.find_spec("torch")
+    return os.path.dirname(spec.origin) if spec else ""
+
+
+def calls_need() -> str:
+    """What is missing here to build the extension module; empty: nothing."""
+    torch_dir = _torch_dir()
+    for what, there in (("g++", shutil.which("g++")), ("torch", torch_dir),
+                        ("Python's headers", os.path.exists(os.path.join(sysconfig.get_paths()["include"], "Python.h"))),
+                        ("torch's headers", os.path.exists(os.path.join(torch_dir, "include", "torch", "csrc", "autograd",
+                                                                        "python_variable.h")))):
+        if not there:
+            return what
+    return ""
+
+
 def _start_calls():
-    torch_dir = os.path.dirname(importlib.util.find_spec("torch").origin)
-    include, lib = os.path.join(torch_dir, "include"), os.path.join(torch_dir, "lib")
+    include, lib = (os.path.join(_torch_dir(), d) for d in ("include", "lib"))
     return _start(["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-I", os.path.join(ROOT, "include"),
                    "-isystem", include, "-isystem", os.path.join(include, "torch", "csrc", "api", "include"),
                    "-isystem", sysconfig.get_paths()["include"]] + CALLS_SOURCES +
                   ["-L" + lib, "-lc10", "-ltorch_cpu", "-ltorch_python"], CALLS)
 
 
-def build(force: bool = False, verbose: bool = False) -> str:
+def build(force: bool = False, verbose: bool = False, calls: bool = True) -> str:
+    """Builds what is missing or stale: the library, and (calls) the extension module, which
+    is left out where there is no compiler, torch or header for it.  What has been built is
+    in place even where the other one fails."""
     running = []
-    if force or stale():
+    if force or stale(LIB):
         cmd = [nvcc(), "-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-lineinfo", "-std=c++17",
                "-Xcompiler", "-fPIC", "-shared", "--threads", "0", "-I", os.path.join(ROOT, "include")] + SOURCES
         if verbose:
             cmd.insert(1, "-Xptxas=-v")
         running.append(_start(cmd, LIB))
-    # (without torch there is the library alone)
-    if importlib.util.find_spec("torch") and (force or stale(CALLS, CALLS_SOURCES + HEADERS[:1])):
+    if calls and not calls_need() and (force or stale(CALLS, CALLS_SOURCES + HEADERS[:1])):
         running.append(_start_calls())
-    failed = [p.args for p, _, _ in running if p.wait()]
+    failed = []
+    for p, tmp, target in running:
+        if p.wait():
+            failed.append(p)
+        else:
+            os.replace(tmp, target)
     if failed:
-        raise subprocess.CalledProcessError(1, failed[0])
-    for _, tmp, target in running:
-        os.replace(tmp, target)
+        raise subprocess.CalledProcessError(failed[0].returncode, failed[0].args)
     return LIB
 
 
