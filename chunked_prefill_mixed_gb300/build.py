@@ -2,6 +2,7 @@
 Python side's extension module with g++ against the installed torch."""
 from __future__ import annotations
 
+import importlib.metadata
 import importlib.util
 import os
 import shutil
@@ -16,7 +17,19 @@ SOURCES = [os.path.join(HERE, "csrc", f) for f in ("plan.cpp", "mixed_attn.cu", 
                                                         "rope_append.cu", "paged_attn.cu")]
 HEADERS = [os.path.join(ROOT, "include", "sarathi.h")] + [
     os.path.join(HERE, "csrc", f) for f in ("sarathi_internal.h", "paged_internal.h", "device_util.cuh")]
-CALLS = os.path.join(HERE, "_paged_calls.so")
+
+
+def calls_path() -> str:
+    """Where the extension module is: named by what it is built against, so that one of
+    another Python or torch is not taken for it."""
+    try:
+        torch = importlib.metadata.version("torch")
+    except importlib.metadata.PackageNotFoundError:
+        torch = "none"
+    return os.path.join(HERE, f"_paged_calls.{sys.implementation.cache_tag}-torch{torch}.so")
+
+
+CALLS = calls_path()
 CALLS_SOURCES = [os.path.join(HERE, "csrc", "paged_calls.cpp")]
 
 

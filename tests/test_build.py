@@ -84,3 +84,19 @@ def test_loading_the_library_does_not_need_the_module(tools, monkeypatch):
         S.load()
     with pytest.raises(ImportError, match="Python's headers"):
         S.paged_calls()
+
+
+@needs_torch
+def test_the_module_is_built_again_for_another_torch_or_python(monkeypatch):
+    import importlib.metadata
+    import torch
+    now = B.calls_path()
+    assert now == B.CALLS and os.path.dirname(now) == os.path.dirname(B.LIB)
+    assert torch.__version__.split("+")[0] in now
+    real = importlib.metadata.version
+    with monkeypatch.context() as m:
+        m.setattr(importlib.metadata, "version", lambda name: "99.1" if name == "torch" else real(name))
+        assert B.calls_path() != now
+    with monkeypatch.context() as m:
+        m.setattr(B.sys.implementation, "cache_tag", "cpython-399")
+        assert B.calls_path() != now
