@@ -182,7 +182,9 @@ class PagedPlan:
 class PagedRunner:
     """The paged operators of one attention shape on one device: owns the RoPE
     table and the workspaces, plans batches and enqueues the calls on ``stream``
-    (default: the device's current stream).
+    (default: the device's current stream).  dtype: the element type of every call's
+    tensors, which are refused where they are of another; None: each call's own, bf16 or
+    fp16.
 
     Calls on different streams get workspaces of their own.  Calls captured into
     CUDA graphs use the runner's main workspace, sized when a batch is planned
@@ -190,7 +192,7 @@ class PagedRunner:
     replayed at the same time as one another, or as its calls outside graphs on
     its first stream, and the runner has to live as long as they do."""
 
-    def __init__(self, H_q: int, H_kv: int, d: int, dtype=torch.bfloat16, device="cuda", max_pos: int = 0,
+    def __init__(self, H_q: int, H_kv: int, d: int, dtype=None, device="cuda", max_pos: int = 0,
                  rope_theta: float = 10000.0, page_size: int = 16, rope_style: int = 0):
         self.shape = Shape(H_q, H_kv, d, page_size)
         self.dtype = dtype
@@ -280,10 +282,16 @@ class PagedRunner:
                     w = self._others[raw] = torch.zeros(size, dtype=torch.uint8, device=self.device)
         return raw, w
 
+    def _typed(self, name: str, t) -> None:
+        if getattr(t, "dtype", self.dtype) != self.dtype:
+            raise ValueError(f"{name}: {t.dtype}, and the runner is for {self.dtype}")
+
     def append(self, k, v, k_cache, v_cache, slots, positions, q=None, q_out=None, sections=None, stream=None) -> None:
         """Rotate and store the new tokens' keys and values (sarathi_rope_append)."""
         if self.rope is None:
             raise ValueError("the runner has no RoPE table: give it max_pos")
+        if self.dtype is not None:
+            self._typed("k", k)
         raw, workspace = self._on(stream, 256)
         _made(self._calls.append, "sarathi_rope_append", self._append, self.device.index, workspace, k, v, k_cache, v_cache,
               slots, positions, q, q_out, sections, raw)
@@ -291,6 +299,8 @@ class PagedRunner:
     def attend(self, plan: PagedPlan, q, k_cache, v_cache, out, score_cap: float = 0.0, slopes=None, lse=None,
                stream=None, sm_scale: float | None = None) -> None:
         """Attention of a planned batch (sarathi_paged_attn)."""
+        if self.dtype is not None:
+            self._typed("q", q)
         raw, workspace = self._on(stream, plan.workspace_bytes)
         if raw != plan.home and (workspace is not self.workspace or not self._capturing(
                 raw, torch._C._cuda_getCurrentRawStream(self.device.index))):

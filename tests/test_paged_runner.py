@@ -66,6 +66,7 @@ def made(monkeypatch):
         r = object.__new__(M.PagedRunner)
         r.device, r._home, r._retired, r._others = torch.device("cuda", 0), home, [], {}
         r._lock, r.workspace, r.rope, r.shape = threading.Lock(), torch.empty(1 << 16, dtype=torch.uint8), Memory(), None
+        r.dtype = None
         r._calls, r._append = SimpleNamespace(attend="attend", append="append"), None
         monkeypatch.setattr(M, "_made", lambda call, *a: calls.append((call, a)))
         return r, Cuda(monkeypatch), calls
@@ -143,3 +144,25 @@ def test_a_capture_is_seen_from_another_device(made, call_on, given):
     cuda.device, cuda.current, cuda.captured = 1, call_on, {call_on}
     r.attend(_plan(0x10), None, None, None, None, stream=call_on if given else None)
     assert calls[-1][1][4] is r.workspace and not r._others and cuda.device == 1
+
+
+def test_tensors_of_another_type_than_the_runners_are_refused(made):
+    """A runner for one element type takes that one (the other tensors have to be of the
+    same as the first anyway); a runner for none takes both."""
+    r, cuda, calls = made(0x10)
+    cuda.current = 0x10
+    bf, half = (torch.zeros(1, dtype=t) for t in (torch.bfloat16, torch.float16))
+
+    def both(t):
+        r.append(t, t, None, None, None, None)
+        r.attend(_plan(0x10), t, None, None, None)
+    both(bf), both(half)
+    for mine, other in ((bf, half), (half, bf)):
+        r.dtype = mine.dtype
+        both(mine)
+        n = len(calls)
+        with pytest.raises(ValueError, match="k: .*the runner is for"):
+            r.append(other, other, None, None, None, None)
+        with pytest.raises(ValueError, match="q: .*the runner is for"):
+            r.attend(_plan(0x10), other, None, None, None)
+        assert len(calls) == n
