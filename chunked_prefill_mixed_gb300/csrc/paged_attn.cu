@@ -59,7 +59,7 @@ struct Params {
     const int32_t* plan;
     int off_pages, off_tokens, off_items, off_merge;
     int n_items, n_first, first_sms, n_merge;
-    int num_tokens, Hq, Hkv, group, num_pages;
+    int Hq, Hkv, group, num_pages;
     float raw_scale;  // of q . K: sm_scale log2(e), or sm_scale / cap under a cap
     float cap2;       // cap log2(e); 0: no cap
     int cap_fine;     // the cap is above kCapFine
@@ -1554,7 +1554,6 @@ extern "C" int32_t sarathi_paged_attn(const sarathi_paged_args* a, void* cuda_st
     P.n_items = in->n_items;
     P.n_first = in->n_first;
     P.n_merge = in->n_merge;
-    P.num_tokens = in->num_tokens;
     P.Hq = Hq;
     P.Hkv = Hkv;
     P.group = Hq / Hkv;
