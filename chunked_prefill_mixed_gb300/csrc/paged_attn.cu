@@ -7,13 +7,14 @@
 // queues:
 //
 //   TILE    up to two tiles of 128 query rows (token x q head of one kv head's
-//           group) over a range of keys in 128-key blocks: a chunk's tokens over
-//           their row's pages, or all the tokens of a group of requests over the
-//           pages that they share.  S = Q K^T and O += P V run on the tensor
-//           cores (tcgen05, accumulators and P in tensor memory), K and V come
-//           by TMA straight from the pages, and each tile's softmax is done by a
-//           warpgroup of its own, one thread a row, so that one tile's
-//           exponentials run while the other tile's products do.
+//           group) over a range of keys in blocks (80 keys at d = 128, 128 at
+//           d = 64): a chunk's tokens over their row's pages, or all the
+//           tokens of a group of requests over the pages that they share.  S
+//           = Q K^T and O += P V run on the tensor cores (tcgen05,
+//           accumulators and P in tensor memory), K and V come by TMA straight
+//           from the pages, and each tile's softmax is done by a warpgroup of
+//           its own, one thread a row, so that one tile's exponentials run
+//           while the other tile's products do.
 //   STREAM  a range of a one-token row's pages for one kv head, by one warp:
 //           TMA page loads that run on into the warp's next item, warp-level MMA
 //           for the 16 padded rows of a group.  The bytes are the bound there,
@@ -25,9 +26,10 @@
 //
 // What bounds them, on a GB300 that copies at 6.8 TB/s and multiplies bf16 at 1.9
 // PFLOP/s: streams, HBM (80 decodes of 32 / 8 heads, 732 MB, 116 us, 6.3 TB/s);
-// tiles of long chunks, the softmax beside the products (4096-token prompt, 32 / 8
-// heads, d 128, 1.27 PFLOP/s; 2048 tokens behind 6144 keys with a bias, 202 us, 1.19
-// PFLOP/s, the tensor pipe active in 60% of the cycles); short key ranges, 1.5 us
+// tiles of long chunks, softmax and products that overlap in part only (pages in
+// order: 4096-token prompt, 32 / 8 heads, d 128, 106 us, 1.30 PFLOP/s; 2048 tokens
+// behind 6144 keys with a bias, 200 us, 1.20 PFLOP/s, the tensor pipe active in 60% of
+// the cycles, and 250 us with scattered pages, a copy each); short key ranges, 1.5 us
 // an item beside 1 to 1.7 us a block (4001 tokens of 9 documents, 29 us).
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -71,8 +73,8 @@ struct Params {
 
 constexpr int kThreads = 384;      // 12 warps: 0-7 softmax / streams, 8-11 copies and MMA issue
 constexpr int kMainThreads = 256;
-// Registers: a softmax thread holds its row's 128 scores.  Both shares together
-// are what the block is launched with (384 x 168): 256 x 216 + 128 x 72.
+// Registers: a softmax thread holds its row's 80 or 128 scores of a block.  Both
+// shares together are what the block is launched with (384 x 168): 256 x 216 + 128 x 72.
 constexpr int kMainRegs = 216, kAuxRegs = 72, kLaunchRegs = 168;
 static_assert(kMainThreads * kMainRegs + (kThreads - kMainThreads) * kAuxRegs <= kThreads * kLaunchRegs,
               "register split");
@@ -476,10 +478,10 @@ __device__ void tile_clean(const Params& P, const Tile& T, const Counts& c, uint
 // A warp takes it where all of a block's scores allow; scales whose seventh power
 // would leave fp32 do not.  The scores of keys that a row does not see are left out:
 // past an item's last key they are products with whatever the ring held, and the
-// formulas differ in the last bits.  That is looked at only where the block's
-// largest score of all is above the first bound: the maximum of the seen ones costs
-// as much again (80 keys of 128 rows with a window of 500, 41.9 us; in every block with
-// a hidden key 46.5).  Left to each row instead of to the warp, 1.15 to 1.4 times the time.
+// formulas differ in the last bits.  The maximum of the seen ones is taken only
+// where the block's largest score of all is above the first bound: the same tokens
+// with a window of 500 take 41.9 us, 46.5 where every block with a hidden key takes
+// it.  A choice by row instead of by warp takes 1.15 to 1.4 times as long.
 constexpr float kTanhLow = 0.35f, kTanhHigh = 0.6f;
 constexpr float kScaleLow = 2e-4f, kScaleHigh = 50.f;
 struct CapPoly {
@@ -524,7 +526,7 @@ __device__ __forceinline__ uint32_t bit_range(int a, int z) {
 // ---------------------------------------------------------------------------
 // What a tile's scores may be, as far as a kernel knows.  The code of other kinds
 // costs time even where no call takes it: 2048 tokens behind 6144 keys with a bias
-// take 202 us with a kernel of their own, 217 with the one for all; 2048 behind 2048
+// take 200 us with a kernel of their own, 217 with the one for all; 2048 behind 2048
 // at d = 64 64 us plain (70) and 83 biased (87).  Plain scores at d = 128 (95 against
 // 91 us) and capped ones (2% less) have none.
 enum Scores { kAny = 0, kBiased = 1, kPlain = 2 };
